@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "grad_signals.cuh"
 #include "kernels.h"
 #include "row_slice.cuh"
 
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kStreamThreads, kGrad ? 4 : 8) distill_stream_
 // Each is a named barrier (passed an mbarrier, so that A, who is seldom late, need
 // not be waited for) in two sets, one for the rows of either parity.  A waits for
 // passed(n) before it signals row n + 2: none is signalled again before all have
-// passed it.  Waits for copies and for other CTAs end after 2 s;
+// passed it.  What orders the rows of one slice: grad_signals.cuh.  Waits for copies and for other CTAs end after 2 s;
 // the cluster's rows from there on report DSPARK_REQ_TIMEOUT.
 //
 // Bound by memory: 7,168 bf16 rows of 129,280 take 547 us, 3.71 GB read and written
@@ -481,7 +482,6 @@ __global__ void __launch_bounds__(kStreamThreads, kGrad ? 4 : 8) distill_stream_
 // the two passes in turn, 702 us (the stores came in bursts); slices held in
 // registers, 957; the gradient written over the logits and copied out in bulk, 779
 // (the slice is occupied longer).
-constexpr int kSlices = 3;
 constexpr int kLosses = 8;  // rows whose shares of the loss may be on their way
 constexpr int kSets = 4;    // rows between warps A's, the newest, and warps C's
 
@@ -496,7 +496,7 @@ struct Place {  // where a row's slice lies: vectors in it, its first element, t
 
 template <int kGroupWarps>
 struct GradShared {
-    uint64_t full[kSlices];     // a slice has arrived
+    uint64_t full[kFull];       // a row's slice has arrived
     uint64_t passed[2];         // a row of either parity is past its scalars
     uint64_t parts_in[4];       // every CTA's part has
     uint64_t loss_in[kLosses];  // rank 0's: every CTA's share of the loss has
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
     const float a = kLog2e * p.inv_t;
 
     if (tid == 0) {
-        for (int i = 0; i < kSlices; ++i) mbar_init(&sh.full[i], 1);
+        for (int i = 0; i < kFull; ++i) mbar_init(&sh.full[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&sh.passed[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&sh.parts_in[i], 1);
         for (int i = 0; i < kLosses; ++i) mbar_init(&sh.loss_in[i], 1);
@@ -558,14 +558,14 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
         const int edge_slot = (t & 7) + (t & 32) / 4;
 #pragma unroll 1
         for (int n = own; n < rows; n += 2) {
-            uint4* const slice = reinterpret_cast<uint4*>(s_dyn + n % kSlices * kSliceBytes);
+            uint4* const slice = reinterpret_cast<uint4*>(s_dyn + slice_of(n) * kSliceBytes);
             bar_sync(kBarReady + own, kGroup + 32);
             const Place g = sh.place[n & 7];
             const bool masked = sh.weight[n & 3] == 0.0f;
             // this thread's element of the edge, if it holds one (threads 0..7 and 32..39 of rank 0)
             int edge_at = -1;
             if (rank == 0) edge_at = t < g.head ? t : t >= 32 && t - 32 < p.V - g.tail0 ? g.tail0 + t - 32 : -1;
-            const float edge = edge_at >= 0 ? sh.edge[n % kSlices][edge_slot] : neg_inf();
+            const float edge = edge_at >= 0 ? sh.edge[slice_of(n)][edge_slot] : neg_inf();
             if (!masked) {
                 constexpr int kBatch = kNV < 8 ? kNV : 8;
                 Running run;
@@ -626,11 +626,10 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
         // out of the instruction caches)
         const int own = warp - kGradWarps;  // takes the rows of this parity
         uint32_t* const s_mark = s_marks + own * kMarkWords;
-        int stuck = -1;  // the slice whose copy this lane gave up waiting for
-        uint32_t stuck_parity = 0;
+        int stuck = -1;  // the row whose copy this lane gave up waiting for
 #pragma unroll 1
         for (int n = own; n < rows; n += 2) {
-            const int at = n % kSlices;
+            const int at = slice_of(n);
             const int64_t row = row0 + n * step;
             const Slice<kDtype> s(p.draft, row, p.row_stride, p.V, rank, C);
             const float w = load_weight(p, row);
@@ -660,11 +659,9 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
             }
             // row n - 2 is past its scalars: all have passed what is signalled below
             if (n > 1 && !sh.timeout && !mbar_wait(&sh.passed[own], (n / 2 - 1) & 1, kWaitLimitNs)) sh.timeout = 1;
-            const uint32_t parity = n / kSlices & 1;
-            if (!sh.timeout && !mbar_wait(&sh.full[at], parity, kWaitLimitNs)) {  // no copy is started after a timeout
-                sh.timeout = 1;
-                stuck = at;
-                stuck_parity = parity;
+            if (!sh.timeout && !mbar_wait(&sh.full[full_of(n)], full_parity(n), kWaitLimitNs)) {
+                sh.timeout = 1;  // no copy is started from here on
+                stuck = n;
             }
             // ---- the slice is there
             float* const edge = sh.edge[at];
@@ -706,7 +703,7 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
             bar_arrive(kBarEntries + own, 64);
         }
         // a copy whose wait gave up may still be in flight: this shared memory is its target
-        if (stuck >= 0) mbar_wait(&sh.full[stuck], stuck_parity, kWaitLimitNs);
+        if (stuck >= 0) mbar_wait(&sh.full[full_of(stuck)], full_parity(stuck), kWaitLimitNs);
     } else if (warp < kGradWarps + 4) {
         // ------------------------------------------------------------ warps B
         const int own = warp - kGradWarps - 2;
@@ -831,18 +828,18 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
         write_loss(n - 2);
     } else {
         // ------------------------------------------------------------- warp D
-        // one arrival on the slice's mbarrier for every row, with or without a copy
+        // one arrival on the row's mbarrier, with or without a copy
         auto copy = [&](int n, float w) {
             if (lane != 0 || n >= rows) return;
             const Slice<kDtype> s(p.draft, row0 + n * step, p.row_stride, p.V, rank, C);
             sh.place[n & 7] = Place{s.count, s.elem0, s.head, s.tail0};
-            uint64_t* const full = &sh.full[n % kSlices];
+            uint64_t* const full = &sh.full[full_of(n)];
             if (w == 0.0f || s.count == 0 || sh.timeout) {
                 mbar_arrive(full);
                 return;
             }
             mbar_arrive_expect_tx(full, s.count * 16);
-            bulk_g2s(s_dyn + n % kSlices * kSliceBytes, s.vec(0), s.count * 16, full);
+            bulk_g2s(s_dyn + slice_of(n) * kSliceBytes, s.vec(0), s.count * 16, full);
         };
         auto weight = [&](int n) { return n < rows ? load_weight(p, row0 + n * step) : 0.0f; };
         copy(0, weight(0));
