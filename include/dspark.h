@@ -551,8 +551,8 @@ int dspark_distill_loss(const void* draft, int dtype, int64_t row_stride, const 
  *   grad        [N, V] out, contiguous, of the draft's type (rounded once).
  *               Rows of weight 0 and rows that keep no entry get zeros; rows
  *               whose loss is NaN get NaN.
- *   status      as for dspark_distill_loss, and DSPARK_REQ_TIMEOUT (loss and
- *               gradient NaN) for rows whose kernel gave up a wait.
+ *   status      as for dspark_distill_loss, and DSPARK_REQ_TIMEOUT (loss NaN,
+ *               gradient not to be used) for rows whose kernel gave up a wait.
  * No workspace.
  */
 int dspark_distill_grad(const void* draft, int dtype, int64_t row_stride, const void* values,

@@ -470,11 +470,16 @@ __global__ void __launch_bounds__(kStreamThreads, kGrad ? 4 : 8) distill_stream_
 //   passed(n)   C -> A             the row is past them
 //   stored(n)   workers -> C, D    the gradient is stored, the slice free
 //
-// Each is a named barrier (passed an mbarrier, so that A, who is seldom late, need
-// not be waited for) in two sets, one for the rows of either parity.  A waits for
-// passed(n) before it signals row n + 2: none is signalled again before all have
-// passed it.  What orders the rows of one slice: grad_signals.cuh.  Waits for copies and for other CTAs end after 2 s;
-// the cluster's rows from there on report DSPARK_REQ_TIMEOUT.
+// Each is a named barrier in two sets, one for the rows of either parity.  A waits
+// for passed(n) before it signals row n + 2: none is signalled again before all
+// have passed it.  What orders the rows of one slice: grad_signals.cuh.
+//
+// Waits for copies and for other CTAs end after 2 s.  A CTA that gave one up goes
+// through its remaining rows with the barriers above alone: it waits for nothing
+// else, copies nothing and sends the others nothing, so that their waits end too;
+// their rows from there on report DSPARK_REQ_TIMEOUT.  Before it ends, warp D waits
+// again for the copies it had started, and the stores that others may have sent it
+// are given time to arrive.
 //
 // Bound by memory: 7,168 bf16 rows of 129,280 take 547 us, 3.71 GB read and written
 // at 6.8 TB/s, the measured copy bandwidth; 1,792 fp32 rows 292 us, 0.94 of it (a
@@ -484,6 +489,7 @@ __global__ void __launch_bounds__(kStreamThreads, kGrad ? 4 : 8) distill_stream_
 // (the slice is occupied longer).
 constexpr int kLosses = 8;  // rows whose shares of the loss may be on their way
 constexpr int kSets = 4;    // rows between warps A's, the newest, and warps C's
+constexpr uint64_t kLingerNs = 1000000;  // for the last stores sent to a CTA that gave up
 
 struct Kept {  // an entry of the list on its way from warp A to warp C
     int id;    // of this slice, or -1
@@ -497,7 +503,6 @@ struct Place {  // where a row's slice lies: vectors in it, its first element, t
 template <int kGroupWarps>
 struct GradShared {
     uint64_t full[kFull];       // a row's slice has arrived
-    uint64_t passed[2];         // a row of either parity is past its scalars
     uint64_t parts_in[4];       // every CTA's part has
     uint64_t loss_in[kLosses];  // rank 0's: every CTA's share of the loss has
     Part part[4][kMaxCluster];
@@ -507,11 +512,16 @@ struct GradShared {
     Row row[4];
     float weight[4];
     float edge[kSlices][16];  // the row's edge: its head, from 8 on its tail
-    Place place[8];
+    Place place[4];
     int timeout;
 };
 
-enum : int { kBarReady = 1, kBarEntries = 3, kBarSums = 5, kBarScalars = 7, kBarStored = 9 };
+enum : int { kBarReady = 1, kBarEntries = 3, kBarSums = 5, kBarScalars = 7, kBarStored = 9, kBarPassed = 11 };
+
+// Whether a wait of this CTA was given up (the same answer in the whole warp).
+__device__ __forceinline__ bool gave_up(const int& timeout) {
+    return __any_sync(0xFFFFFFFFu, *const_cast<const volatile int*>(&timeout));
+}
 
 template <int kDtype, int kWorkers, int kNV>
 constexpr int grad_smem(int K) {
@@ -540,7 +550,6 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
 
     if (tid == 0) {
         for (int i = 0; i < kFull; ++i) mbar_init(&sh.full[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&sh.passed[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&sh.parts_in[i], 1);
         for (int i = 0; i < kLosses; ++i) mbar_init(&sh.loss_in[i], 1);
         fence_mbar_init();
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
         for (int n = own; n < rows; n += 2) {
             uint4* const slice = reinterpret_cast<uint4*>(s_dyn + slice_of(n) * kSliceBytes);
             bar_sync(kBarReady + own, kGroup + 32);
-            const Place g = sh.place[n & 7];
+            const Place g = sh.place[n & 3];
             const bool masked = sh.weight[n & 3] == 0.0f;
             // this thread's element of the edge, if it holds one (threads 0..7 and 32..39 of rank 0)
             int edge_at = -1;
@@ -626,7 +635,6 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
         // out of the instruction caches)
         const int own = warp - kGradWarps;  // takes the rows of this parity
         uint32_t* const s_mark = s_marks + own * kMarkWords;
-        int stuck = -1;  // the row whose copy this lane gave up waiting for
 #pragma unroll 1
         for (int n = own; n < rows; n += 2) {
             const int at = slice_of(n);
@@ -658,15 +666,16 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
                 if (b >= 0) s_mark[b >> 5] = 0u;
             }
             // row n - 2 is past its scalars: all have passed what is signalled below
-            if (n > 1 && !sh.timeout && !mbar_wait(&sh.passed[own], (n / 2 - 1) & 1, kWaitLimitNs)) sh.timeout = 1;
-            if (!sh.timeout && !mbar_wait(&sh.full[full_of(n)], full_parity(n), kWaitLimitNs)) {
-                sh.timeout = 1;  // no copy is started from here on
-                stuck = n;
-            }
+            if (n > 1) bar_sync(kBarPassed + own, 64);
+            if (!gave_up(sh.timeout) && !mbar_wait(&sh.full[full_of(n)], full_parity(n), kWaitLimitNs)) sh.timeout = 1;
+            __syncwarp();
             // ---- the slice is there
             float* const edge = sh.edge[at];
             if (lane < 16) edge[lane] = edge_value;
-            if (lane == 0) sh.weight[n & 3] = w;
+            if (lane == 0) {
+                sh.weight[n & 3] = w;
+                sh.place[n & 3] = Place{s.count, s.elem0, s.head, s.tail0};
+            }
             sh.flags[n & 3][lane] = flags;
             __syncwarp();
             if (w != 0.0f) {
@@ -702,8 +711,6 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
             bar_arrive(kBarReady + own, kGroup + 32);
             bar_arrive(kBarEntries + own, 64);
         }
-        // a copy whose wait gave up may still be in flight: this shared memory is its target
-        if (stuck >= 0) mbar_wait(&sh.full[full_of(stuck)], full_parity(stuck), kWaitLimitNs);
     } else if (warp < kGradWarps + 4) {
         // ------------------------------------------------------------ warps B
         const int own = warp - kGradWarps - 2;
@@ -720,7 +727,8 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
             const int i = n & 3;
             const float w = w_next, lse = lse_next;
             load_row(n + 2);
-            if (lane == 0) mbar_arrive_expect_tx(&sh.parts_in[i], C * 20);
+            const bool expected = !gave_up(sh.timeout);
+            if (expected && lane == 0) mbar_arrive_expect_tx(&sh.parts_in[i], C * 20);
             EntrySums q = kNoEntries;
             if (w != 0.0f) {  // the teacher's sums need no slice
 #pragma unroll 2
@@ -746,18 +754,18 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
             part.m_rest = sh.top[own][lane & (kGroupWarps - 1)];
             part.rest = sh.sum[own][lane & (kGroupWarps - 1)];
             join_lanes<kGroupWarps>(part.m_rest, part.rest, a);
-            part.flags = q.flags | (sh.timeout ? kFlagTimeout : 0);
-            if (lane < C) {
+            part.flags = q.flags;
+            if (!gave_up(sh.timeout) && lane < C) {
                 const uint32_t dst = cluster_addr(&sh.part[i][rank], lane), bar = cluster_addr(&sh.parts_in[i], lane);
                 push_v4(dst, part.m_rest, part.rest, q.m_kept, q.kept, bar);
                 push_u32(dst + 16, static_cast<uint32_t>(part.flags), bar);
             }
-            if (!sh.timeout && !mbar_wait_cluster(&sh.parts_in[i], phase >> i & 1u, kWaitLimitNs)) sh.timeout = 1;
+            if (!gave_up(sh.timeout) && !mbar_wait_cluster(&sh.parts_in[i], phase >> i & 1u, kWaitLimitNs)) sh.timeout = 1;
             phase ^= 1u << i;
             __syncwarp();
             part = Part{kLowest, 0.0f, kLowest, 0.0f, 0};
             if (lane < C) part = sh.part[i][lane];
-            if (sh.timeout) part.flags |= kFlagTimeout;
+            if (gave_up(sh.timeout)) part.flags |= kFlagTimeout;
             Sums g;
             form_sums(p, part, q, w, lse, a, g, sh.row[i]);
             __syncwarp();
@@ -771,14 +779,16 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
         auto write_loss = [&](int n) {
             if (rank != 0 || last_row < 0) return;
             const int i = n & (kLosses - 1);
-            if (!sh.timeout && !mbar_wait_cluster(&sh.loss_in[i], phase >> i & 1u, kWaitLimitNs)) sh.timeout = 1;
+            if (!gave_up(sh.timeout) && !mbar_wait_cluster(&sh.loss_in[i], phase >> i & 1u, kWaitLimitNs)) sh.timeout = 1;
             phase ^= 1u << i;
+            __syncwarp();
+            const bool late = gave_up(sh.timeout);
             if (lane == 0) {
                 const Row& r = sh.row[n & 3];
                 float loss = r.loss_rest;
                 for (int k = 0; k < C; ++k) loss += sh.loss_part[i][k];
-                p.loss[last_row] = r.sums.bad || sh.timeout ? quiet_nan() : r.sums.taught ? loss : 0.0f;
-                p.status[last_row] = sh.timeout ? kReqTimeout : r.sums.code;
+                p.loss[last_row] = r.sums.bad || late ? quiet_nan() : r.sums.taught ? loss : 0.0f;
+                p.status[last_row] = late ? kReqTimeout : r.sums.code;
             }
             __syncwarp();
         };
@@ -796,10 +806,11 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
             const float w = w_next, lse = lse_next;
             load_row(n + 2);
             const int turn = n & (kLosses - 1);
-            if (rank == 0 && lane == 0 && w != 0.0f) mbar_arrive_expect_tx(&sh.loss_in[turn], C * 4);
+            const bool expecting = rank == 0 && w != 0.0f && !gave_up(sh.timeout);
+            if (expecting && lane == 0) mbar_arrive_expect_tx(&sh.loss_in[turn], C * 4);
             write_loss(n - 2);
             bar_sync(kBarScalars + own, kGroup + 64);
-            if (lane == 0) mbar_arrive(&sh.passed[own]);
+            if (n + 2 < rows) bar_arrive(kBarPassed + own, 64);
             Row& r = sh.row[n & 3];
             if (lane == 0 && w != 0.0f) form_loss(p, lse, r);
             __syncwarp();
@@ -816,7 +827,7 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
                     store_elem<kDtype>(grow + static_cast<int64_t>(e.id) * E, entry_grad(p, r, w, e.z, prob, a));
                 }
                 term = warp_sum(term);
-                if (lane == 0)
+                if (!gave_up(sh.timeout) && lane == 0)
                     push_u32(cluster_addr(&sh.loss_part[turn][rank], 0), __float_as_uint(term),
                              cluster_addr(&sh.loss_in[turn], 0));
             } else if (rank == 0 && lane == 0) {
@@ -828,13 +839,14 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
         write_loss(n - 2);
     } else {
         // ------------------------------------------------------------- warp D
+        int begun = 0;  // rows announced
         // one arrival on the row's mbarrier, with or without a copy
         auto copy = [&](int n, float w) {
-            if (lane != 0 || n >= rows) return;
+            if (n >= rows || gave_up(sh.timeout) || lane != 0) return;
+            begun = n + 1;
             const Slice<kDtype> s(p.draft, row0 + n * step, p.row_stride, p.V, rank, C);
-            sh.place[n & 7] = Place{s.count, s.elem0, s.head, s.tail0};
             uint64_t* const full = &sh.full[full_of(n)];
-            if (w == 0.0f || s.count == 0 || sh.timeout) {
+            if (w == 0.0f || s.count == 0) {
                 mbar_arrive(full);
                 return;
             }
@@ -853,9 +865,17 @@ __global__ void __launch_bounds__(kWorkers + 224, kCtas) distill_grad_kernel(con
             bar_sync(kBarStored + (n & 1), kGroup + 64);  // the slice of row n is free
             copy(n + 3, w);
         }
+        // copies that nobody waited for may still be in flight: this shared memory is their target
+        if (gave_up(sh.timeout))
+            for (int n = max(0, begun - kFull); n < begun; ++n)
+                mbar_wait(&sh.full[full_of(n)], full_parity(n), kWaitLimitNs);
     }
     __syncwarp();
     if (C > 1) cluster.sync();  // no CTA leaves while another may still push to it
+    if (gave_up(sh.timeout)) {  // nor before what was pushed, and not waited for, is there
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kLingerNs) {}
+    }
 }
 
 // Clusters of C CTAs of a kernel that can be resident at once (0 if the query fails).
