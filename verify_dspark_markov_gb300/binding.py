@@ -176,19 +176,21 @@ def _stream(stream):
 
 class Workspace:
     """A zero-filled device buffer per (device, op); grown on demand.  The
-    library leaves it zero-filled after every completed call."""
+    library leaves it zero-filled after every completed call.  keep=False: a
+    buffer made now is for this call alone."""
 
     def __init__(self):
         self._bufs = {}
 
-    def get(self, op: int, nbytes: int, device) -> torch.Tensor | None:
+    def get(self, op: int, nbytes: int, device, keep: bool = True) -> torch.Tensor | None:
         if nbytes == 0:
             return None
         key = (torch.device(device).index, op)
         buf = self._bufs.get(key)
         if buf is None or buf.numel() < nbytes:
             buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-            self._bufs[key] = buf
+            if keep:
+                self._bufs[key] = buf
         return buf
 
 
@@ -476,13 +478,19 @@ class _Call:
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def workspace(self, workspace, op, nbytes):
-        # a default workspace per stream: calls on different streams may overlap
-        if workspace is None:
-            workspace, op = _default_ws, (op, self.ptr)
         if self.stream is None:
-            return workspace.get(op, nbytes, self.device)
+            return self._workspace(workspace, op, nbytes)
         with torch.cuda.stream(self.stream):
-            return workspace.get(op, nbytes, self.device)
+            return self._workspace(workspace, op, nbytes)
+
+    def _workspace(self, workspace, op, nbytes):
+        # under capture the zero fill of a new buffer runs with the graph: such a
+        # buffer is that call's alone, and a graph does not share a default one
+        capturing = torch.cuda.is_current_stream_capturing()
+        if workspace is None:
+            # a default workspace per stream: calls on different streams may overlap
+            workspace, op = Workspace() if capturing else _default_ws, (op, self.ptr)
+        return workspace.get(op, nbytes, self.device, keep=not capturing)
 
     def uses(self, *tensors):
         if self.stream is not None:
