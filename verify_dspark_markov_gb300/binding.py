@@ -460,14 +460,19 @@ def _shaped(t, name, dtype, shape, device):
 
 
 class _Call:
-    """The stream of one call.  On a stream other than the current one, what
-    the call allocates belongs to that stream, and the inputs are recorded on
-    it, so that no block is reused while the call may still run."""
+    """The stream of one call, on the current device.  On a stream other than
+    the current one, what the call allocates belongs to that stream, and the
+    inputs are recorded on it, so that no block is reused while the call may
+    still run."""
 
     def __init__(self, stream, device):
+        if device.index != torch.cuda.current_device():  # the library launches there
+            raise ValueError(f"the tensors are on {device}, not on the current device cuda:{torch.cuda.current_device()}")
         self.device = device
         self.ptr = torch._C._cuda_getCurrentRawStream(device.index)  # current_stream() without its object
         self.stream = None
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, not on {device}")
         if stream is not None and stream.cuda_stream != self.ptr:
             self.stream, self.ptr = stream, stream.cuda_stream
 
