@@ -604,7 +604,7 @@ typedef struct {
  *   dst[.., b, j, ..] = src[.., b, parent[b, j], ..]   for every tensor,
  * in one launch (draft or attention states, caches, token histories).
  *   states      n descriptors in HOST memory, 1 <= n <= 16; W beams in src, M
- *               in dst.  src and dst must not overlap.
+ *               in dst.  No dst overlaps a src, parent or another dst.
  *   parent      int32 [B, M]; a value outside [0, W), as an unfilled selection
  *               has, fills its beam with zero bytes.
  */

@@ -673,8 +673,53 @@ def _state(src, dst, dim, name):
 
 def _extent(t):
     """The bytes [first, last) a tensor's elements lie in."""
+    if t.is_contiguous():
+        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
     last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _overlap(a, b):
+    """Whether two tensors may share a byte.  Apart are extents that do not
+    meet, and tensors that lie in different places within every multiple of
+    some stride S (the halves of a double buffer, other positions of a cache):
+    dimensions whose stride is a multiple of S do not move them there."""
+    (a0, a1), (b0, b1) = _extent(a), _extent(b)
+    if a1 <= b0 or b1 <= a0:
+        return False
+    dims = [[(n, s * t.element_size()) for n, s in zip(t.shape, t.stride()) if n > 1] for t in (a, b)]
+    for S in {s for d in dims for _, s in d if s}:
+        wide_a, wide_b = (t.element_size() + sum((n - 1) * s for n, s in d if s % S) for t, d in zip((a, b), dims))
+        apart = (b0 - a0) % S
+        if wide_a <= apart and apart + wide_b <= S:
+            return False
+    return True
+
+
+def _overlaps_itself(t):
+    """Whether a tensor may cover a byte twice (no slice or permutation does)."""
+    span = 1
+    for s, n in sorted((s, n) for n, s in zip(t.shape, t.stride()) if n > 1):
+        if s < span:
+            return True
+        span += (n - 1) * s
+    return False
+
+
+def _refuse_overlaps(states, parent, out):
+    """Outputs share no byte with a state, the parents, another or themselves."""
+    tensors = [parent, *states, *out]
+    spans = [(*_extent(t), i) for i, t in enumerate(tensors) if t.numel()]
+    spans.sort()
+    first_out = 1 + len(states)
+    for at, (_, end, i) in enumerate(spans):
+        if i >= first_out and not tensors[i].is_contiguous() and _overlaps_itself(tensors[i]):
+            raise ValueError(f"out[{i - first_out}] must not overlap itself")
+        for start, _, j in spans[at + 1:]:
+            if start >= end:
+                break
+            if (i >= first_out or j >= first_out) and _overlap(tensors[i], tensors[j]):
+                raise ValueError("out must not overlap the states, the parents or one another")
 
 
 def beam_reorder(states, parent, dim=0, stream=None, out=None):
@@ -683,7 +728,8 @@ def beam_reorder(states, parent, dim=0, stream=None, out=None):
     state[.., b, parent[b, j], ..], all in one launch.  parent: int32 [B, M],
     -1 for an unfilled place (zeros).  A tensor may be a view (the filled part
     of a cache) with one strided dimension on either side of the beams'.  out:
-    None, or the list of tensors to write; they must not overlap the states."""
+    None, or the list of tensors to write, which share no memory with the
+    states, the parents or one another."""
     _dev(parent, "parent", torch.int32)
     if parent.dim() != 2:
         raise ValueError("parent must be [B, M]")
@@ -692,7 +738,7 @@ def beam_reorder(states, parent, dim=0, stream=None, out=None):
     call = _Call(stream, dev)
     if out is not None and len(out) != len(states):
         raise ValueError(f"out must hold {len(states)} tensors")
-    result, words, spans, W = [], [], [], -1
+    result, words, W = [], [], -1
     for i, t in enumerate(states):
         shape = t.shape
         if t.device != dev:
@@ -711,11 +757,8 @@ def beam_reorder(states, parent, dim=0, stream=None, out=None):
         result.append(o)
         if t.numel() and o.numel():
             words += _state(t, o, dim, f"states[{i}]")
-            if out is not None:
-                spans.append((_extent(t), _extent(o)))
-    for _, (lo, hi) in spans:
-        if any(lo < b and a < hi for (a, b), _ in spans):
-            raise ValueError("out must not overlap the states")
+    if out is not None:
+        _refuse_overlaps(states, parent, out)
     lib, most = load(), 13 * MAX_REORDER_STATES
     for at in range(0, len(words), most):
         part = words[at:at + most]
