@@ -755,7 +755,9 @@ def beam_reorder(states, parent, dim=0, stream=None, out=None):
             if o.shape != want or o.dtype != t.dtype or o.device != dev:
                 raise ValueError(f"out[{i}] must be {t.dtype} {want} on {dev}")
         result.append(o)
-        if t.numel() and o.numel():
+        if o.numel():
+            if W == 0:
+                raise ValueError(f"states[{i}] must have at least one beam")
             words += _state(t, o, dim, f"states[{i}]")
     if out is not None:
         _refuse_overlaps(states, parent, out)
