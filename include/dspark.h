@@ -577,7 +577,8 @@ int dspark_distill_grad(const void* draft, int dtype, int64_t row_stride, const 
  *               1 <= M <= DSPARK_MAX_TOP.
  *   out_score, out_parent, out_token  fp32, int32, int32 [B, M] out: score
  *               descending, equal scores by (beam, token) ascending; (-inf, -1,
- *               -1) past the last offered continuation.
+ *               -1) past the last offered continuation.  out_score may be score
+ *               itself (M = W); no other output overlaps an input.
  *   status      int32 [B] out: DSPARK_REQ_EMPTY if nothing is offered;
  *               DSPARK_REQ_NONFINITE for a NaN or +inf score, or logit of a
  *               live beam (the item's outputs are then NaN, -1, -1).

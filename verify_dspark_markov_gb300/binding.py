@@ -600,7 +600,7 @@ def beam_select(logits, scores, m, finished=None, eos=0, workspace: Workspace | 
     whose finished (uint8 [B, W]) is set offers only itself, with token eos; a
     beam of score -inf nothing.  Returns dict(scores fp32, parent int32, token
     int32, each [B, m], status int32 [B]), best first, equal scores by (beam,
-    token); unfilled places are (-inf, -1, -1)."""
+    token); unfilled places are (-inf, -1, -1).  out["scores"] may be `scores`."""
     if logits.dim() != 3:
         raise ValueError("logits must be [B, W, V]")
     if not logits.is_cuda:

@@ -225,11 +225,12 @@ __global__ void __launch_bounds__(kThreads, 6) top_kernel(const TopParams p) {
     uint32_t index0 = 0;   // the first index of this row
     uint64_t* list = nullptr;
     if constexpr (kBeam) {
-        base = __ldg(p.score + row);
+        base = p.score[row];  // out_score may be the same array
         index0 = static_cast<uint32_t>(row % p.W) * p.V;
         list = p.lists + row * p.k;
         const bool ended = p.finished && __ldg(p.finished + row);
         if (bad_logit(base) || base == neg_inf() || ended) {  // no logits to read (the same branch in the whole cluster)
+            sync(cluster, C);  // every CTA has read the score: the last beam to arrive may write over it
             if (rank != 0) return;
             for (int r = tid; r < p.k; r += kThreads) {
                 uint64_t key = 0;
