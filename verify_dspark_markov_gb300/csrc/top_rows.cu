@@ -366,7 +366,10 @@ __global__ void __launch_bounds__(kThreads, 6) top_kernel(const TopParams p) {
         };
         for (int r = count + tid; r < p.k; r += kThreads) put(r, neg_inf(), -1);
         rank_candidates(sh, count, p.k, [&](int r, uint64_t key) {
-            put(r, key_to_float(static_cast<uint32_t>(key >> 32)), 0xFFFFFFFFu - static_cast<uint32_t>(key));
+            const uint32_t id = 0xFFFFFFFFu - static_cast<uint32_t>(key);
+            float v = key_to_float(static_cast<uint32_t>(key >> 32));
+            if (v == 0.0f) v = load_elem<kDtype>(s.row + static_cast<int64_t>(id) * Elem<kDtype>::kSize);  // -0 has 0's key
+            put(r, v, id);
         });
         if (tid == 0) {
             p.lse[row] = bad ? quiet_nan() : empty ? neg_inf() : M * p.inv_t + log_s;
