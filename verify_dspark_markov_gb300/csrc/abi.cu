@@ -159,8 +159,7 @@ int distill_args(DistillParams& p, const void* draft, int dtype, int64_t row_str
     p.V = V;
     p.K = K;
     p.t = temperature;
-    p.inv_t64 = 1.0 / temperature;
-    p.inv_t = static_cast<float>(p.inv_t64);
+    p.inv_t = static_cast<float>(1.0 / temperature);
     p.loss = loss;
     p.status = status;
     return DSPARK_OK;

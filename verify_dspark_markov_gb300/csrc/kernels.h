@@ -326,7 +326,6 @@ struct DistillParams {
     int64_t N;
     int V, K;
     float t, inv_t;            // temperature and 1 / temperature
-    double inv_t64;
     float scale;
     float* loss;               // [N]
     int32_t* status;           // [N]

@@ -387,19 +387,6 @@ __device__ __forceinline__ void join_warps(const float (&w)[kWarps], const float
 __device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
-// Bulk copies shared -> global (both addresses and the size multiples of 16),
-// issued by one thread; their source is free after the first wait, their
-// target written after the second.
-__device__ __forceinline__ void bulk_s2g(void* gdst, const void* smem_src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(gdst),
-                 "r"(smem_u32(smem_src)), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_written() {
-    asm volatile("cp.async.bulk.wait_group 0;\n\tfence.proxy.async.global;" ::: "memory");
-}
-
 // The address of this CTA's shared variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
     uint32_t a;
