@@ -11,7 +11,7 @@ from verify_dspark_markov_gb300 import binding
 
 @pytest.fixture
 def devices(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 100 + index)
 
 

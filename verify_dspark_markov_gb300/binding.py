@@ -466,8 +466,9 @@ class _Call:
     still run."""
 
     def __init__(self, stream, device):
-        if device.index != torch.cuda.current_device():  # the library launches there
-            raise ValueError(f"the tensors are on {device}, not on the current device cuda:{torch.cuda.current_device()}")
+        current = torch._C._cuda_getDevice()  # torch.cuda.current_device() without its checks; the library launches there
+        if device.index != current:
+            raise ValueError(f"the tensors are on {device}, not on the current device cuda:{current}")
         self.device = device
         self.ptr = torch._C._cuda_getCurrentRawStream(device.index)  # current_stream() without its object
         self.stream = None
@@ -483,12 +484,9 @@ class _Call:
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def workspace(self, workspace, op, nbytes):
-        if self.stream is None:
-            return self._workspace(workspace, op, nbytes)
-        with torch.cuda.stream(self.stream):
-            return self._workspace(workspace, op, nbytes)
-
-    def _workspace(self, workspace, op, nbytes):
+        if self.stream is not None and self.stream.cuda_stream != torch._C._cuda_getCurrentRawStream(self.device.index):
+            with torch.cuda.stream(self.stream):
+                return self.workspace(workspace, op, nbytes)
         # under capture the zero fill of a new buffer runs with the graph: such a
         # buffer is that call's alone, and a graph does not share a default one
         capturing = torch.cuda.is_current_stream_capturing()
