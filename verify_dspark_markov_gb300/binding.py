@@ -493,7 +493,11 @@ class _Call:
         if workspace is None:
             # a default workspace per stream: calls on different streams may overlap
             workspace, op = Workspace() if capturing else _default_ws, (op, self.ptr)
-        return workspace.get(op, nbytes, self.device, keep=not capturing)
+            return workspace.get(op, nbytes, self.device, keep=not capturing)
+        buf = workspace.get(op, nbytes, self.device, keep=not capturing)
+        if buf is not None and buf.is_cuda:  # a call on another stream may have made it
+            buf.record_stream(self.stream or torch.cuda.current_stream(self.device))
+        return buf
 
     def uses(self, *tensors):
         if self.stream is not None:
