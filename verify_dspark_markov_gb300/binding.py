@@ -176,8 +176,10 @@ def _stream(stream):
 
 class Workspace:
     """A zero-filled device buffer per (device, op); grown on demand.  The
-    library leaves it zero-filled after every completed call.  keep=False: a
-    buffer made now is for this call alone."""
+    library leaves it zero-filled after every completed call.  For calls that a
+    graph captures, one that an earlier call used: without it the graph fills
+    its own at every replay.  keep=False: a buffer made now is for this call
+    alone."""
 
     def __init__(self):
         self._bufs = {}
