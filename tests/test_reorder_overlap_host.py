@@ -75,3 +75,20 @@ def test_what_is_refused(which, monkeypatch):
                    "parent": ([torch.empty((2, 3), dtype=torch.int32)], [parent])}[which]
     with pytest.raises(ValueError, match="overlap"):
         binding.beam_reorder(states, parent, out=out)
+
+
+def test_spans_of_a_descriptor():
+    """The bytes that a state's descriptor spans are its tensor's."""
+    rng = random.Random(2)
+    for _ in range(300):
+        outer, inner = rng.choice([(), (3,)]), rng.choice([(), (5,), (2, 6), (4, 3, 2)])
+        B, W, M = rng.randint(1, 3), rng.randint(1, 3), rng.randint(1, 3)
+        cut = (slice(None),) * (len(outer) + 2) + (slice(rng.randrange(2), None),) * min(1, len(inner))
+        t = torch.empty((*outer, B, W, *inner), dtype=torch.int32)[cut]
+        o = torch.empty((*outer, B, M, *inner), dtype=torch.int32)[cut]
+        read, written, once = binding._spans(binding._state(t, o, len(outer), "t"), B, W, M)
+        assert read == binding._extent(t) and written == binding._extent(o)
+        assert once and not binding._overlaps_itself(o)
+        if M > 1:
+            twice = o.narrow(len(outer) + 1, 0, 1).expand(o.shape)
+            assert not binding._spans(binding._state(t, twice, len(outer), "t"), B, W, M)[2]

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 import struct
 import threading
@@ -638,6 +639,9 @@ def beam_select(logits, scores, m, finished=None, eos=0, workspace: Workspace | 
     return out
 
 
+_first = operator.itemgetter(0)
+
+
 def _collapse(dims):
     """Dimensions (size, source stride, target stride), outermost first, as few
     as describe the same elements."""
@@ -677,8 +681,6 @@ def _state(src, dst, dim, name):
 
 def _extent(t):
     """The bytes [first, last) a tensor's elements lie in."""
-    if t.is_contiguous():
-        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
     last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
 
@@ -710,19 +712,28 @@ def _overlaps_itself(t):
     return False
 
 
-def _refuse_overlaps(states, parent, out):
-    """Outputs share no byte with a state, the parents, another or themselves."""
-    tensors = [parent, *states, *out]
-    spans = [(*_extent(t), i) for i, t in enumerate(tensors) if t.numel()]
-    spans.sort()
-    first_out = 1 + len(states)
-    for at, (_, end, i) in enumerate(spans):
-        if i >= first_out and not tensors[i].is_contiguous() and _overlaps_itself(tensors[i]):
-            raise ValueError(f"out[{i - first_out}] must not overlap itself")
-        for start, _, j in spans[at + 1:]:
+def _spans(words, B, W, M):
+    """The bytes [first, last) of a dspark_state's source and target, and
+    whether the target's strides, each past what the ones after it span, say
+    that it covers none of them twice."""
+    src, dst, run, on, mn, so, si, sb, sm, to, ti, tb, tm = words
+    mid = run + (mn - 1) * tm
+    beams = mid + (M - 1) * tb
+    item = beams + (B - 1) * ti
+    once = (mn == 1 or tm >= run) and (M == 1 or tb >= mid) and (B == 1 or ti >= beams) and (on == 1 or to >= item)
+    return (src, src + run + (mn - 1) * sm + (W - 1) * sb + (B - 1) * si + (on - 1) * so), \
+        (dst, dst + item + (on - 1) * to), once
+
+
+def _refuse_overlaps(spans):
+    """spans: (first, last, whether it is written, tensor).  What is written
+    shares no byte with anything else."""
+    spans.sort(key=_first)
+    for at, (_, end, written, t) in enumerate(spans):
+        for start, _, other_written, other in spans[at + 1:]:
             if start >= end:
                 break
-            if (i >= first_out or j >= first_out) and _overlap(tensors[i], tensors[j]):
+            if (written or other_written) and _overlap(t, other):
                 raise ValueError("out must not overlap the states, the parents or one another")
 
 
@@ -742,7 +753,7 @@ def beam_reorder(states, parent, dim=0, stream=None, out=None):
     call = _Call(stream, dev)
     if out is not None and len(out) != len(states):
         raise ValueError(f"out must hold {len(states)} tensors")
-    result, words, W = [], [], -1
+    result, words, spans, W = [], [], [], -1
     for i, t in enumerate(states):
         shape = t.shape
         if t.device != dev:
@@ -762,9 +773,17 @@ def beam_reorder(states, parent, dim=0, stream=None, out=None):
         if o.numel():
             if W == 0:
                 raise ValueError(f"states[{i}] must have at least one beam")
-            words += _state(t, o, dim, f"states[{i}]")
-    if out is not None:
-        _refuse_overlaps(states, parent, out)
+            state = _state(t, o, dim, f"states[{i}]")
+            words += state
+            if out is not None:
+                read, written, once = _spans(state, B, W, M)
+                if not once and _overlaps_itself(o):
+                    raise ValueError(f"out[{i}] must not overlap itself")
+                spans += (*read, False, t), (*written, True, o)
+    if spans:
+        at = parent.data_ptr()
+        spans.append((at, at + 4 * B * M, False, parent))
+        _refuse_overlaps(spans)
     lib, most = load(), 13 * MAX_REORDER_STATES
     for at in range(0, len(words), most):
         part = words[at:at + most]
